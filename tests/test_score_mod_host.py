@@ -190,3 +190,14 @@ def test_layouts_round_trip():
     assert torch.equal(R.from_seq(R.to_seq(x, 4)), x)
     assert torch.equal(R.from_head(R.to_head(x, 4)), x)
     assert torch.equal(R.from_head(R.to_head(x, 4, 2), 2), x)
+
+
+# ------------------------------------------------------------ read, not run
+
+def test_barriers_behind_divergent_code_are_not_the_aligned_kind():
+    """barrier.cluster's .aligned forms are defined only where a warp's lanes
+    arrive together; the plan's kernel reaches its barriers from per-lane
+    branches and a search whose length differs from lane to lane."""
+    with open(os.path.join(B.CSRC, "mask.cu")) as f:
+        asm = [line for line in f if "asm volatile" in line and "barrier.cluster" in line]
+    assert asm and not any(".aligned" in line for line in asm)

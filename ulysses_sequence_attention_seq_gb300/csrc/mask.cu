@@ -343,8 +343,10 @@ __global__ void __launch_bounds__(256) mask_order_kernel(const BuildParams p) {
 // above take as long one behind the other, but 21 us called one by one.
 constexpr int kMiddle = 8 * kSmall;
 
+// (Every thread of the block calls it, but after branches that differ from lane to
+// lane: so not the .aligned forms, which want a warp's lanes together.)
 __device__ __forceinline__ void cluster_barrier() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
 __global__ void __launch_bounds__(kSmall) mask_cluster_kernel(const BuildParams p) {
