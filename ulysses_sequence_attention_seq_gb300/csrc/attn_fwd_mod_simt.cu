@@ -190,6 +190,13 @@ __global__ void __launch_bounds__(32 * kWarps) attn_fwd_mod_simt_kernel(const Si
 #pragma unroll
           for (int jj = 0; jj < nJ; jj += 4) {
             dev::f2x x = dev::f2_of(s[i][jj], s[i][jj + 1]), y = dev::f2_of(s[i][jj + 2], s[i][jj + 3]);
+            uint32_t seen = 0;  // (what is unseen may be NaN, and four scores share a reciprocal)
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+              const int key = k0 + tk + 4 * (jj + n);
+              if (key >= lo[i] && key < hi[i]) seen |= 1u << n;
+            }
+            cap.drop_unseen(x, y, seen);
             cap(x, y);
             const float2 x2 = dev::f2_to(x), y2 = dev::f2_to(y);
             s[i][jj] = x2.x, s[i][jj + 1] = x2.y, s[i][jj + 2] = y2.x, s[i][jj + 3] = y2.y;

@@ -526,7 +526,11 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, 1)
               for (int e = 0; e < 8; e += 2) {
                 f2x v[2] = {f2_of(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])),
                             f2_of(__uint_as_float(s[2 * e + 2]), __uint_as_float(s[2 * e + 3]))};
-                if constexpr (kForm == 2) any(v[0], v[1]);
+                if constexpr (kForm == 2) {
+                  // (four scores share a reciprocal, and what is unseen may be NaN)
+                  if constexpr (kMask) any.drop_unseen(v[0], v[1], seen >> (2 * e));
+                  any(v[0], v[1]);
+                }
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                   if constexpr (kForm < 2) {
@@ -629,17 +633,20 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, 1)
           // logits in place first, masked ones -inf.
           bool raw = (kCap || kBias) && !part && lb.ok && !__any_sync(0xffffffffu, m_used == -INFINITY);
           auto make_logits = [&]() { dev::logits<kMod>(s, p.mod, sl2, slope2, kv0 - pos); };
-          if (!raw) {
-            make_logits();
-            if (part) {
+          auto put_unseen = [&](float value) {
 #pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                const uint32_t seen = bits_of(c0 - 32 * c, c1 - 32 * c);
+            for (int c = 0; c < 4; ++c) {
+              const uint32_t seen = bits_of(c0 - 32 * c, c1 - 32 * c);
 #pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  if (!(seen & (1u << e))) s[c][e] = __float_as_uint(-INFINITY);
-              }
+              for (int e = 0; e < 32; ++e)
+                if (!(seen & (1u << e))) s[c][e] = __float_as_uint(value);
             }
+          };
+          if (!raw) {
+            // (the cap's exponential form mixes four scores, and what is unseen may be NaN)
+            if (kCap && part) put_unseen(0.f);
+            make_logits();
+            if (part) put_unseen(-INFINITY);
           }
           // Row maximum: eight independent chains of three-input maxima over 16 columns each.
           auto row_max = [&]() -> float {

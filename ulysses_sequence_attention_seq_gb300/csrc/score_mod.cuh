@@ -11,7 +11,8 @@
 //               instructions a pair of scores on top of the plain softmax's,
 //   |y| <= 0.6  the same to y^8, 7.4e-8: five,
 //   any         1 - 2 / (1 + exp(2 y)) with the hardware's exp2, and one
-//               hardware reciprocal for four scores (of their product).
+//               hardware reciprocal for four scores (of their product; so the
+//               forwards, whose unseen keys may be NaN, put 0 for their scores).
 // The polynomials interpolate tanh(sqrt z) / sqrt z at the Chebyshev points of
 // the interval in z = y^2 and are applied to the raw q.k: scale, cap and
 // log2(e) are in the coefficients.  The forward, which has its scores in
@@ -142,6 +143,16 @@ struct CapAny {
     const f2x r2 = f2_mul(f2_of(r, r), f2_of(t.y, t.x));  // 1 / (a.x b.x), 1 / (a.y b.y)
     s0 = f2_fma(f2_mul(r2, b), n, c);
     s1 = f2_fma(f2_mul(r2, a), n, c);
+  }
+  // 0 for those of four scores whose bit of `seen` is off: the others would take
+  // NaN from the product that the reciprocal is of.
+  static __device__ __forceinline__ void drop_unseen(f2x &s0, f2x &s1, uint32_t seen) {
+    float2 a = f2_to(s0), b = f2_to(s1);
+    if (!(seen & 1u)) a.x = 0.f;
+    if (!(seen & 2u)) a.y = 0.f;
+    if (!(seen & 4u)) b.x = 0.f;
+    if (!(seen & 8u)) b.y = 0.f;
+    s0 = f2_of(a.x, a.y), s1 = f2_of(b.x, b.y);
   }
 };
 
