@@ -2,8 +2,11 @@
 points (fake pointers, never dereferenced), the plan's size, the Python
 layer's checks, and the float64 forms the GPU tests rely on (modref.py)
 against differences and worked examples."""
+import copy
 import ctypes
+import dataclasses
 import os
+import pickle
 
 import pytest
 import torch
@@ -190,6 +193,17 @@ def test_layouts_round_trip():
     assert torch.equal(R.from_seq(R.to_seq(x, 4)), x)
     assert torch.equal(R.from_head(R.to_head(x, 4)), x)
     assert torch.equal(R.from_head(R.to_head(x, 4, 2), 2), x)
+
+
+def test_a_used_problem_copies_and_pickles(lib):
+    p = prob(S=64, n_head=8, n_kv_head=8, hidden=1024)
+    t = torch.empty(8, 1, 8, 8, 128, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        U.ulysses_attn_fwd_mod(p, t, t, t, U.ScoreMod(), t, t, t)   # (works out the problem's sizes, then refuses)
+    for q in (copy.copy(p), copy.deepcopy(p), pickle.loads(pickle.dumps(p)), dataclasses.replace(p)):
+        assert q == p and hash(q) == hash(p) and vars(q) == dataclasses.asdict(p)
+        with pytest.raises(ValueError):
+            U.ulysses_attn_fwd_mod(q, t, t, t, U.ScoreMod(), t, t, t)
 
 
 # ------------------------------------------------------------ read, not run

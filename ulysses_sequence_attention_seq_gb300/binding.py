@@ -103,6 +103,11 @@ class Problem:
         n_kv_head < Pu (each kv-head then replicated to Pu / n_kv_head ranks)."""
         return self.n_kv_head // self.Pu if self.n_kv_head >= self.Pu else 1
 
+    def __getstate__(self):
+        """The fields alone: what calls have worked out (_facts) holds addresses of
+        this process and stays out of copies and pickles."""
+        return {k: v for k, v in self.__dict__.items() if k != "_facts"}
+
     def scale(self) -> float:
         return self.softmax_scale if self.softmax_scale > 0 else 1.0 / math.sqrt(self.head_dim)
 
