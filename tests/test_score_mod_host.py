@@ -206,6 +206,29 @@ def test_a_used_problem_copies_and_pickles(lib):
             U.ulysses_attn_fwd_mod(q, t, t, t, U.ScoreMod(), t, t, t)
 
 
+def test_a_layer_step_makes_no_buffer(lib, monkeypatch):
+    """Everything a step writes is there before it, made on the stream that made
+    the rest: a block the allocator hands out in the middle of a step belongs to
+    the current stream, and the step may run on another."""
+    p = prob(B=1, S=16, hidden=1024, n_head=8, n_kv_head=8)
+    b = U.Buffers(p, device="cpu", backward=True)
+    calls = []
+    for name in ("ulysses_pack_qkv", "ulysses_qk_norm_pack", "ulysses_attn_fwd_mod", "ulysses_unpack_out",
+                 "ulysses_attn_bwd_mod", "ulysses_qk_norm_bwd"):
+        monkeypatch.setattr(U, name, lambda *a, name=name: calls.append((name, a)))
+    for name in ("empty", "empty_like", "zeros", "zeros_like"):
+        monkeypatch.setattr(torch, name, lambda *a, **k: pytest.fail("a tensor is made"))
+    norm, stream = (None, None, 1e-6), object()
+    b.forward_mod(U.ScoreMod(), norm, stream)
+    b.backward_mod(U.ScoreMod(), norm, None, stream)
+    assert [c[0] for c in calls] == ["ulysses_qk_norm_pack", "ulysses_attn_fwd_mod", "ulysses_unpack_out",
+                                     "ulysses_attn_bwd_mod", "ulysses_qk_norm_bwd"]
+    assert all(c[1][-1] is stream for c in calls)
+    between = [t.data_ptr() for t in calls[3][1][8:10]]
+    assert between == [t.data_ptr() for t in calls[4][1][6:8]]
+    assert len({*between, b.dq_seq.data_ptr(), b.dk_seq.data_ptr()}) == 4
+
+
 # ------------------------------------------------------------ read, not run
 
 def test_barriers_behind_divergent_code_are_not_the_aligned_kind():

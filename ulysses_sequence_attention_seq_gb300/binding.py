@@ -576,6 +576,9 @@ class Buffers:
             self.dq_seq = e(p.P, p.B, p.Sl, p.n_head, D)
             self.dk_seq = e(p.P, p.B, p.Sl, p.n_kv_head, D)
             self.dv_seq = e(p.P, p.B, p.Sl, p.n_kv_head, D)
+            # gradients between the attention's backward and the norms'
+            self.dqn_seq = e(p.P, p.B, p.Sl, p.n_head, D)
+            self.dkn_seq = e(p.P, p.B, p.Sl, p.n_kv_head, D)
         # phase 2 (the fused backward's dQ accumulator) and phase 3 (the dS
         # store) when asked for
         phases = [1] + [2] * fused + [3] * ds if backward else [0]
@@ -615,18 +618,12 @@ class Buffers:
         inputs end up in dq_seq and dk_seq too and those of the weights in
         dnorm = (dq_weight, dk_weight), float32 or None."""
         p = self.prob
-        dq, dk = (self.dq_seq, self.dk_seq) if norm is None else self._norm_grads()
+        dq, dk = (self.dq_seq, self.dk_seq) if norm is None else (self.dqn_seq, self.dkn_seq)
         ulysses_attn_bwd_mod(p, self.q_head, self.k_head, self.v_head, self.o_head, self.lse, self.do_seq, mod, dq, dk,
                              self.dv_seq, self.ws, stream)
         if norm is not None:
             ulysses_qk_norm_bwd(p, self.q_seq, self.k_seq, *norm, dq, dk, self.dq_seq, self.dk_seq,
                                 *(dnorm or (None, None)), self.ws, mod.mask, stream)
-
-    def _norm_grads(self):
-        """Buffers for the gradients between the attention and the norms (made on first use)."""
-        if not hasattr(self, "dqn_seq"):
-            self.dqn_seq, self.dkn_seq = torch.empty_like(self.dq_seq), torch.empty_like(self.dk_seq)
-        return self.dqn_seq, self.dkn_seq
 
     def backward_fused(self, stream=None):
         ulysses_attn_bwd_fused(self.prob, self.q_head, self.k_head, self.v_head, self.o_head, self.lse,
