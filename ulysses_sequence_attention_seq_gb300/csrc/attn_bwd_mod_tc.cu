@@ -1063,8 +1063,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr bool kBias = (kMod & kModBias) != 0;
     // What an item's row needs from global memory beside its tiles: its factors
     // (nlse, delta) and the keys it sees, {first, how many}.
-    float nl2, dlt;
-    int2 keys;
+    // (As of an empty row until an item with keys comes.)
+    float nl2 = 0.f, dlt = 0.f;
+    int2 keys = make_int2(0, 0);
     // Starts an item: brings these, and (warpgroup 0) this thread's Q row or
     // (warpgroup 1) its dO row, into TMEM (rows past S are zero).  The item
     // before has formed its last S and dP.
