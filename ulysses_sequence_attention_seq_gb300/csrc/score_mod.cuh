@@ -11,8 +11,8 @@
 //               instructions a pair of scores on top of the plain softmax's,
 //   |y| <= 0.6  the same to y^8, 7.4e-8: five,
 //   any         1 - 2 / (1 + exp(2 y)) with the hardware's exp2, and one
-//               hardware reciprocal for four scores (of their product; so the
-//               forwards, whose unseen keys may be NaN, put 0 for their scores).
+//               hardware reciprocal for four scores (of their product; so where
+//               unseen keys of a forward give NaN, 0 is put for their scores).
 // The polynomials interpolate tanh(sqrt z) / sqrt z at the Chebyshev points of
 // the interval in z = y^2 and are applied to the raw q.k: scale, cap and
 // log2(e) are in the coefficients.  The forward, which has its scores in
@@ -224,6 +224,23 @@ __device__ __forceinline__ int cap_form(float big, const ScoreMod &m) {
   return __any_sync(0xffffffffu, big > m.lim4) ? 2 : 1;
 }
 
+// Raw scores on their way to the exponential form, where four share a
+// reciprocal: if any of the warp's is NaN, 0 for those whose bit of `seen` is off
+// (keys of padding may hold anything).
+template <int n>
+__device__ __forceinline__ void drop_unseen_nan(uint32_t (&s)[n], uint32_t seen) {
+  f2x sum = f2_of(0.f, 0.f);
+#pragma unroll
+  for (int e = 0; e < n; e += 2) sum = f2_add(sum, f2_of(__uint_as_float(s[e]), __uint_as_float(s[e + 1])));
+  const float2 sum2 = f2_to(sum);
+  const float all = sum2.x + sum2.y;  // (NaN of infinities of both signs, too)
+  if (__any_sync(0xffffffffu, all != all)) {
+#pragma unroll
+    for (int e = 0; e < n; ++e)
+      if (!(seen & (1u << e))) s[e] = 0u;
+  }
+}
+
 // The bias -slope |lead + c| (base 2) of score c = 0, 1, ..: `lead` is the
 // position of the first score a thread holds minus the fixed position of its
 // row (or key), so key and query side read the same.  Linear in c, slope2 c +
@@ -250,11 +267,19 @@ struct BiasSteps {
   }
 };
 
+// Bits [lo, hi) of a word (either may lie outside it).
+__device__ __forceinline__ uint32_t bits_of(int lo, int hi) {
+  const uint32_t below = hi >= 32 ? 0xffffffffu : hi <= 0 ? 0u : (1u << hi) - 1u;
+  return lo <= 0 ? below : lo >= 32 ? 0u : below & (0xffffffffu << lo);
+}
+
 // Base-2 logits in place of the raw scores a thread holds, 32 to a row of `s`,
-// any size, any side of the diagonal.
+// any size, any side of the diagonal.  `part`: some of the warp's keys, outside
+// [lo, hi), are not seen; what becomes of their scores does not matter, but it
+// stays with them.
 template <int kMod, int kRows>
 __device__ __forceinline__ void logits(uint32_t (&s)[kRows][32], const ScoreMod &m, float scale_log2, float slope2,
-                                       int lead) {
+                                       int lead, bool part, int lo, int hi) {
   const float lf = (float)lead;
   if constexpr ((kMod & kModCap) != 0) {
     // (The exponential form is off by some 2^-22 of the cap however small the
@@ -267,6 +292,7 @@ __device__ __forceinline__ void logits(uint32_t (&s)[kRows][32], const ScoreMod 
         big = sm100::max3(big, fabsf(__uint_as_float(s[r][e])), fabsf(__uint_as_float(s[r][e + 1])));
       if (__any_sync(0xffffffffu, big * big > m.lim4)) {
         const CapAny cap(m);
+        if (part) drop_unseen_nan(s[r], bits_of(lo - 32 * r, hi - 32 * r));
 #pragma unroll
         for (int e = 0; e < 32; e += 4) {
           f2x x = f2_of(__uint_as_float(s[r][e]), __uint_as_float(s[r][e + 1]));

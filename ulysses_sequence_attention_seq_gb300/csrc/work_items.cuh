@@ -61,11 +61,5 @@ __device__ __forceinline__ Item get_item(uint32_t at) {
   return it;
 }
 
-// Bits [lo, hi) of a word (either may lie outside it).
-__device__ __forceinline__ uint32_t bits_of(int lo, int hi) {
-  const uint32_t below = hi >= 32 ? 0xffffffffu : hi <= 0 ? 0u : (1u << hi) - 1u;
-  return lo <= 0 ? below : lo >= 32 ? 0u : below & (0xffffffffu << lo);
-}
-
 }  // namespace dev
 }  // namespace ulysses
