@@ -54,3 +54,33 @@ def test_padding_may_hold_anything(c):
         _, o, lse = forward(prob, x, mod, ws)
         R.assert_within(R.from_head(o.cpu()), val["o"], bnd["o"], f"o, k {k_fill}")
         R.assert_within(R.lse_from_head(lse.cpu()), val["lse"], bnd["lse"], f"lse, k {k_fill}")
+
+
+def test_plans_of_other_sizes_are_told_apart():
+    """A plan says which sizes it is of in full.  (257, 1024) and (1, 125184) are two
+    that a 32-bit hash of batch, length and flag took for one; the buffer has room
+    for both."""
+    small = dict(n_head=1, n_kv_head=1, head_dim=64, hidden=64, P=1, use_rope=False)
+    made, used = U.Problem(B=257, S=1024, **small), U.Problem(B=1, S=125184, **small)
+    n = max(U.ulysses_mask_bytes(made), U.ulysses_mask_bytes(used))
+    plan = torch.empty(n, dtype=torch.uint8, device="cuda")
+    U.ulysses_mask_build(made, None, None, 100, plan)
+    ws = workspace(used, 1)
+    q, k, v, o = (torch.zeros(1, 1, used.S, 1, 64, dtype=torch.bfloat16, device="cuda") for _ in range(4))
+    lse = torch.zeros(1, 1, 1, used.S, device="cuda")
+    g = [torch.full_like(q, 5.0) for _ in range(3)]
+    o.fill_(3.0), lse.fill_(3.0)
+    mod = U.ScoreMod(mask=plan)
+    U.ulysses_qk_norm_pack(used, q, k, v, None, None, 1e-6, plan, *g, ws)
+    assert U.ulysses_read_status(ws) == U.STATUS_MASK and all((t == 5.0).all() for t in g)
+    U.ulysses_workspace_init(used, ws)
+    U.ulysses_attn_fwd_mod(used, q, k, v, mod, o, lse, ws)
+    assert U.ulysses_read_status(ws) == U.STATUS_MASK and (o == 3.0).all() and (lse == 3.0).all()
+    U.ulysses_workspace_init(used, ws)
+    U.ulysses_attn_bwd_mod(used, q, k, v, o, lse, torch.zeros(1, 1, used.S, 64, dtype=torch.bfloat16, device="cuda"),
+                           mod, *g, ws)
+    assert U.ulysses_read_status(ws) == U.STATUS_MASK and all((t == 5.0).all() for t in g)
+    U.ulysses_workspace_init(used, ws)
+    U.ulysses_mask_build(used, None, None, 100, plan)      # and the same buffer with a plan of its own
+    U.ulysses_attn_fwd_mod(used, q, k, v, mod, o, lse, ws)
+    assert U.ulysses_read_status(ws) == 0 and (o == 0.0).all()

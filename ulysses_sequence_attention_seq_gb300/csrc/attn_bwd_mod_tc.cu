@@ -104,7 +104,8 @@ __device__ __forceinline__ int hl_outer(const BwdParams &p, int rb, int pos) {
 // What a block looks at before it starts: the status word, the RoPE table's key
 // and the plan's key, read together (each is a trip to L2).
 struct Checks {
-  uint32_t status, rope, mask;
+  uint32_t status, rope;
+  uint64_t mask;
   __device__ __forceinline__ explicit Checks(const BwdParams &p) {
     const volatile uint32_t *st = p.status;
     status = st[0], rope = st[1], mask = dev::mask_key_of(p.mod.mask);

@@ -35,15 +35,15 @@ struct MaskView {
   const int *col_n;      // [B][n_t] query tiles that see a key tile ...
   const uint16_t *cols;  // [B][n_t][n_t] ... in rising order: 2 * tile + (nothing of the pair needs masking)
   const int2 *order;     // [B][n_t] {key tile, its query tiles}, those with most first
-  const uint32_t *head;  // {key}
-  uint32_t key;
+  const uint64_t *head;  // {key}
+  uint64_t key;          // B, S and the causal flag themselves: no two problems share one
   int Sp, n_t;
   long long rows_n;      // B * Sp
 };
 
 // The plan's key: not m.key where it was built for another problem.  (Read it
 // first and look at it once the block's other loads are on their way.)
-__device__ __forceinline__ uint32_t mask_key_of(const MaskView &m) { return m.ranges ? __ldg(m.head) : m.key; }
+__device__ __forceinline__ uint64_t mask_key_of(const MaskView &m) { return m.ranges ? __ldg(m.head) : m.key; }
 __device__ __forceinline__ bool mask_matches(const MaskView &m) { return mask_key_of(m) == m.key; }
 
 __device__ __forceinline__ bool row_empty(const MaskView &m, int b, int pos, uint32_t *status) {
