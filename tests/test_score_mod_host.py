@@ -238,3 +238,14 @@ def test_barriers_behind_divergent_code_are_not_the_aligned_kind():
     with open(os.path.join(B.CSRC, "mask.cu")) as f:
         asm = [line for line in f if "asm volatile" in line and "barrier.cluster" in line]
     assert asm and not any(".aligned" in line for line in asm)
+
+
+@pytest.mark.parametrize("name", ["attn_fwd_mod_tc.cu", "attn_bwd_mod_tc.cu", "attn_fwd_mod_simt.cu"])
+def test_reads_of_the_plan_ask_in_a_checked_build(name):
+    """Entries of the plan, and slopes, are read behind in_range, there or in the
+    helpers of mask.cuh and score_mod.cuh."""
+    with open(os.path.join(B.CSRC, name)) as f:
+        lines = f.read().split("\n")
+    for i, line in enumerate(lines):
+        if "__ldg(" in line and ("mask." in line or "slopes" in line or "list" in line or "__ldg(tl" in line):
+            assert "in_range" in " ".join(lines[max(0, i - 1):i + 1]), f"{name}:{i + 1}"

@@ -377,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int kl = hid % p.kvp, rb = hid / p.kvp;
   // the key tile (low ones have the most work under the causal flag), its query tiles
   int2 mine = make_int2(ht.rank, p.causal ? n_qt - ht.rank : n_qt);
-  if (p.mod.mask.ranges) mine = __ldg(p.mod.mask.order + (long long)(rb % p.B) * n_qt + ht.rank);
+  if (p.mod.mask.ranges) mine = dev::order_at(p.mod.mask, (long long)(rb % p.B) * n_qt + ht.rank, p.status);
   if (!checks.fine(p)) return;
   if (pad + L::kUsed > L::kAlloc) {  // uniform over the block: nobody has touched a barrier yet
     if (threadIdx.x == 0) atomicOr(p.status, (uint32_t)ULYSSES_STATUS_SMEM_ALIGN);
@@ -408,7 +408,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const int n_iter = p.group * n_m;
   // the query tile of step i
-  auto tile_of = [&](int i) -> int { return list ? __ldg(list + i % n_m) >> 1 : m0 + i % n_m; };
+  auto tile_of = [&](int i) -> int {
+    return list ? dev::col_at(p.mod.mask, list, i % n_m, p.status) >> 1 : m0 + i % n_m;
+  };
 
   if (threadIdx.x == 0) {
     mbar_init(bar + kKBarIn, 1);
@@ -613,7 +615,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t w[2][16];
       float slope2 = 0.f;
       if constexpr ((kMod & kModBias) != 0)
-        slope2 = __ldg(p.mod.slopes + (rb / p.B) * p.hp + kl * p.group + i / n_m) * kLog2e;
+        slope2 = in_range(p.status, (rb / p.B) * p.hp + kl * p.group + i / n_m, 1, p.n_head)
+                     ? __ldg(p.mod.slopes + (rb / p.B) * p.hp + kl * p.group + i / n_m) * kLog2e
+                     : 0.f;
       const float big = p_mod<kMod, kForm, true, kMask>(
           sr, tools, p.scale_log2, slope2, q0 - kvr, side, [&](int c) { return dev::f2_of(nl2[c].x, nl2[c].y); }, lo,
           k_cnt, pf, w);
@@ -679,7 +683,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int q0 = (m0 + i % n_m) * 128 + g * 64;
         bool whole = false;  // mask plan: nothing of the tile pair is masked
         if (list) {
-          const int e = __ldg(list + i % n_m);
+          const int e = dev::col_at(p.mod.mask, list, i % n_m, p.status);
           q0 = (e >> 1) * 128 + g * 64;
           whole = e & 1;
         }
@@ -830,7 +834,7 @@ __device__ __forceinline__ Item dq_item(const BwdParams &p, int block) {
   it.t0 = it.nA = 0;
   it.nB = p.causal ? min(n_qt, it.tile + 1) : n_qt;
   if (p.mod.mask.ranges) {
-    const int4 tl = __ldg(p.mod.mask.tiles + (long long)(it.rb % p.B) * n_qt + it.tile);
+    const int4 tl = dev::tile_at(p.mod.mask, (long long)(it.rb % p.B) * n_qt + it.tile, p.status);
     it.t0 = tl.x / 128;
     it.nB = max((tl.y + 127) / 128 - it.t0, 0);
   }
@@ -1131,7 +1135,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       {
         const Item it = get_item(item_slot(n));
         end = i + it.nB, koff = (it.t0 - i) * 128 + g * 64, qi = it.tile * 128 + r, zero = it.zero;
-        if constexpr (kBias) slope2 = __ldg(p.mod.slopes + (it.rb / p.B) * p.hp + it.j) * kLog2e;
+        if constexpr (kBias) slope2 = dev::slope_at(p.mod, (it.rb / p.B) * p.hp + it.j, p.n_head, p.status);
         if (turns(qi))
           rope_prefetch(p.rope_cos + (size_t)qi * (D / 2) + g * 32, p.rope_sin + (size_t)qi * (D / 2) + g * 32);
       }

@@ -48,7 +48,7 @@ struct Tile {
 struct SimtParams {
   const float *q, *k, *v;
   float *o, *lse;
-  int S, B, hp, kvp, group, causal;
+  int S, B, n_head, hp, kvp, group, causal;
   float scale_log2;
   uint32_t *status;
   long long qo_n, kv_n, lse_n;
@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(32 * kWarps) attn_fwd_mod_simt_kernel(const Si
     hi[i] = __shfl_sync(0xffffffffu, r_hi, tq + 8 * i);
   }
   float slope2 = 0.f;
-  if (p.mod.slopes) slope2 = __ldg(p.mod.slopes + (rb / p.B) * p.hp + j) * 1.4426950408889634f;
+  if (p.mod.slopes) slope2 = dev::slope_at(p.mod, (int)(rb / p.B) * p.hp + j, p.n_head, p.status);
 
   for (int i = threadIdx.x; i < kRows * (D / 4); i += 32 * kWarps) {
     const int r = i / (D / 4), c = i % (D / 4);
@@ -343,7 +343,7 @@ cudaError_t launch_attn_fwd_mod_simt(const ulysses_problem &p, const float *q, c
                                      cudaStream_t st) {
   SimtParams sp{};
   sp.q = q, sp.k = k, sp.v = v, sp.o = o, sp.lse = lse;
-  sp.S = p.S, sp.B = p.B, sp.hp = p.n_head / p.P, sp.kvp = kv_per_rank(p), sp.group = sp.hp / sp.kvp;
+  sp.S = p.S, sp.B = p.B, sp.n_head = p.n_head, sp.hp = p.n_head / p.P, sp.kvp = kv_per_rank(p), sp.group = sp.hp / sp.kvp;
   sp.causal = p.causal;
   const float scale = p.softmax_scale > 0.f ? p.softmax_scale : 1.0f / sqrtf((float)p.head_dim);
   sp.scale_log2 = scale * 1.4426950408889634f;

@@ -172,8 +172,9 @@ __device__ __forceinline__ Item item_of(const FwdParams &p, int block) {
   const int n_kt = (p.S + BN - 1) / BN, m = 2 * it.tile;
   it.t0 = 0;
   if (p.mod.mask.ranges) {
-    const int4 *tl = p.mod.mask.tiles + (long long)(it.rb % p.B) * n_kt;
-    const int4 ta = __ldg(tl + m), tb = m + 1 < n_kt ? __ldg(tl + m + 1) : make_int4(INT_MAX, 0, 0, 0);
+    const long long at = (long long)(it.rb % p.B) * n_kt + m;
+    const int4 ta = dev::tile_at(p.mod.mask, at, p.status);
+    const int4 tb = m + 1 < n_kt ? dev::tile_at(p.mod.mask, at + 1, p.status) : make_int4(INT_MAX, 0, 0, 0);
     it.t0 = min(ta.x, tb.x) / BN;  // (INT_MAX: nothing is seen, nB is 0 below)
     const int endA = (ta.y + BN - 1) / BN, endB = (tb.y + BN - 1) / BN;
     it.nB = max(max(endA, endB) - it.t0, 0);
@@ -612,7 +613,7 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, 1)
         // the scale of what exps reads: raw scores, or (capped, biased) base-2 logits
         const float xs = kCap || kBias ? 1.0f : sl2;
         float slope2 = 0.f;
-        if constexpr (kBias) slope2 = __ldg(p.mod.slopes + (it.rb / p.B) * p.hp + it.j) * 1.4426950408889634f;
+        if constexpr (kBias) slope2 = dev::slope_at(p.mod, (it.rb / p.B) * p.hp + it.j, p.Pu * p.hp, p.status);
         for (int t = 0; t < n_mine; ++t) {
           if (!warp_wait(bar + kBarSFull + 8 * x, (done + t) & 1, abort_flag, gst)) {
             ok = false;

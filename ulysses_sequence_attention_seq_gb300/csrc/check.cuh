@@ -1,7 +1,9 @@
 // check.cuh -- the range checks of a checked build.
 //
 // Compiled with -DULYSSES_CHECK_BOUNDS, every plain global load and store a
-// kernel makes (the TMA's tensor copies check their own bounds in hardware)
+// kernel makes (the TMA's tensor copies check their own bounds in hardware; the
+// kernels that build the mask plan, mask.cu, have no status word and do not ask,
+// those that read it do; loops over an array's own length do not ask either)
 // first asks in_range whether the elements [first, first + count) lie inside
 // the buffer's [0, limit).  A failed check sets ULYSSES_STATUS_BOUNDS in the
 // status word (when the kernel has one) and the access is skipped: no trap,

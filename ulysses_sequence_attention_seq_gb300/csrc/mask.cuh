@@ -52,6 +52,19 @@ __device__ __forceinline__ bool row_empty(const MaskView &m, int b, int pos, uin
   return !in_range(status, i, 1, m.rows_n) || __ldg(&m.ranges[i].y) == 0;
 }
 
+// Entries of the plan, range-checked in a checked build: query tile i's
+// {hull, common keys} and the i-th key tile in order (both of B * n_t), and entry
+// i of the lists (B * n_t * n_t).
+__device__ __forceinline__ int4 tile_at(const MaskView &m, long long i, uint32_t *status) {
+  return in_range(status, i, 1, m.rows_n / 128) ? __ldg(m.tiles + i) : make_int4(INT_MAX, 0, INT_MAX, 0);
+}
+__device__ __forceinline__ int2 order_at(const MaskView &m, long long i, uint32_t *status) {
+  return in_range(status, i, 1, m.rows_n / 128) ? __ldg(m.order + i) : make_int2(0, 0);
+}
+__device__ __forceinline__ int col_at(const MaskView &m, const uint16_t *list, int i, uint32_t *status) {
+  return in_range(status, list - m.cols + i, 1, m.rows_n / 128 * m.n_t) ? __ldg(list + i) : 0;
+}
+
 }  // namespace dev
 
 // Byte offsets inside a mask plan (256-aligned; the first 256 bytes: the key).

@@ -101,7 +101,7 @@ struct NormParams {
   uint32_t *status;
   uint32_t rope_key;
   dev::MaskView mask;       // rows that see nothing: written as zeros (null: none)
-  long long q_n, k_n, qh_n, kh_n, rope_n;
+  long long q_n, k_n, qh_n, kh_n, rope_n, part_n;
 };
 
 // Token row (s*B + b)*Sl + t of the sequence layout.
@@ -490,7 +490,8 @@ __global__ void __launch_bounds__(32 * kWarps) qk_norm_bwd_kernel(const NormPara
       float sum = 0.f;
       for (int th = cc; th < kThreads; th += lanes) sum += red[th][i];
       if (gridDim.x > 1) {
-        p.part[((long long)blockIdx.x * 2 + which) * p.D + e] = sum;
+        const long long at = ((long long)blockIdx.x * 2 + which) * p.D + e;
+        if (in_range(p.status, at, 1, p.part_n)) p.part[at] = sum;
       } else {
         (which ? p.dwk : p.dwq)[e] = sum;
       }
@@ -643,6 +644,7 @@ cudaError_t launch_qk_norm_bwd(const ulysses_problem &p, const void *q, const vo
   const WorkspaceLayout L = workspace_layout(p);
   const long long max_parts = (long long)((L.total_bwd - L.dohead) / ((size_t)2 * p.head_dim * 4));
   n.part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + L.dohead);
+  n.part_n = (long long)((L.total_bwd - L.dohead) / sizeof(float));
   return p.dtype == ULYSSES_BF16 ? launch_bwd<__nv_bfloat16>(p, n, dwq, dwk, max_parts, st)
                                  : launch_bwd<float>(p, n, dwq, dwk, max_parts, st);
 }

@@ -241,6 +241,11 @@ __device__ __forceinline__ void drop_unseen_nan(uint32_t (&s)[n], uint32_t seen)
   }
 }
 
+// Head h's slope, for base-2 logits.
+__device__ __forceinline__ float slope_at(const ScoreMod &m, int h, int n_head, uint32_t *status) {
+  return in_range(status, h, 1, n_head) ? __ldg(m.slopes + h) * 1.4426950408889634f : 0.f;
+}
+
 // The bias -slope |lead + c| (base 2) of score c = 0, 1, ..: `lead` is the
 // position of the first score a thread holds minus the fixed position of its
 // row (or key), so key and query side read the same.  Linear in c, slope2 c +
