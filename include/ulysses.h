@@ -538,7 +538,8 @@ int ulysses_mask_build(const ulysses_problem *prob, const int32_t *doc, const in
  *   x = c - slopes[h] * |i - k|  (h the global q-head);  P_i = softmax of x_i
  *   over the keys that row i sees by the mask plan (NULL: by prob->causal).
  * softcap: 0, or from 2^-10 to 2^20 (else ULYSSES_ERR_ARG).  slopes: device,
- * float [n_head].  mask: a plan of ulysses_mask_build with mask_bytes bytes
+ * float [n_head], on a 16-byte boundary like every pointer (a slice of a larger
+ * array that is not: ULYSSES_ERR_ALIGN).  mask: a plan of ulysses_mask_build with mask_bytes bytes
  * (too few: ULYSSES_ERR_WORKSPACE).
  */
 typedef struct ulysses_score_mod {
@@ -553,7 +554,11 @@ typedef struct ulysses_score_mod {
  * LSE = -infinity.  With `mod` all off this is ulysses_attn_fwd.  Types, head
  * dimensions, layouts, ring and errors as there.  v of tokens that no row sees
  * is multiplied by zero, so it must be finite (ulysses_qk_norm_pack writes zeros
- * there); q and k there may be anything.  A plan built for another problem sets
+ * there, ulysses_pack_qkv copies what it finds); q and k there may be anything,
+ * NaN and infinities too.  bf16 capped at up to 55 without a bias: exp(capped
+ * score) is summed as it is, so S e^softcap |v| has to stay below 3e38 and
+ * e^-softcap |v|, where it matters, above 1e-38 (at 50 and 64K tokens: |v| from
+ * 1e-16 to 1e12).  A plan built for another problem sets
  * ULYSSES_STATUS_MASK and leaves the outputs unwritten.  Accuracy of the cap:
  * 4e-7 of the capped score where |s| is within 0.6 softcap for all the scores
  * that a warp looks at together (for softcap * sqrt(head_dim) above about 10^4

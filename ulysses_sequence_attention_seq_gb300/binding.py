@@ -120,8 +120,9 @@ class CScoreMod(ctypes.Structure):
 @dataclasses.dataclass(frozen=True)
 class ScoreMod:
     """Mirror of ``ulysses_score_mod``: scores capped at ``softcap`` by tanh (0:
-    not), ``-slopes[h] * |i - k|`` added ([n_head] float32), keys by the plan in
-    ``mask`` (a byte tensor built by ulysses_mask_build)."""
+    not), ``-slopes[h] * |i - k|`` added ([n_head] float32, on a 16-byte boundary:
+    clone a slice), keys by the plan in ``mask`` (a byte tensor built by
+    ulysses_mask_build)."""
     softcap: float = 0.0
     slopes: Optional[torch.Tensor] = None
     mask: Optional[torch.Tensor] = None
@@ -602,7 +603,10 @@ class Buffers:
 
     def forward_mod(self, mod: ScoreMod, norm=None, stream=None):
         """The forward with modified scores; norm: None, or (q_weight, k_weight,
-        eps) of the query/key norms.  The norms' pack reads mod's mask too."""
+        eps) of the query/key norms.  The norms' pack reads mod's mask too and
+        writes zeros for padding, whatever it holds; without norms padding is
+        packed as it is, and v_seq has to be finite there (for backward_mod q_seq
+        and k_seq, too)."""
         p = self.prob
         if norm is None:
             ulysses_pack_qkv(p, self.q_seq, self.k_seq, self.v_seq, self.q_head, self.k_head, self.v_head, self.ws,

@@ -32,7 +32,7 @@
 //   - dQ's blocks go on with items of blocks that have not started
 //     (work_items.cuh): the next rows of Q and dO go to tensor memory, and its
 //     first S and dP are formed, during this item's epilogue.  8K tokens x 32
-//     heads of 128 in documents of 1024: dQ 185 -> 161 us.  (dK/dV has 3.4 items
+//     heads of 128 in equal documents of 1024: dQ 185 -> 161 us.  (dK/dV has 3.4 items
 //     an SM there, four times as long each, and its K and V tiles fill shared
 //     memory to the end of an item.)
 // What bounds them is, as in the plain kernels, the chain from scores to P to dS
@@ -40,7 +40,7 @@
 // warp for a capped score.  32K tokens x 8 heads of 128, causal, capped at 50:
 // 5700 us, of which the packing of dO 85 (0.71 of the measured bf16 rate for the
 // 7 products); 8K tokens x 32 heads in documents of about 2048, capped at 50:
-// 602 us, mask only 519 us.
+// 602 us, mask only 519 us (617 us where they lie less well).
 #include <cuda_bf16.h>
 #include <math.h>
 #include <stdint.h>

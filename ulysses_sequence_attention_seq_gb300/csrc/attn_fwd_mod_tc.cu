@@ -34,8 +34,10 @@
 // have not started (work_items.cuh): the next item's Q, K and V are loaded and
 // its first scores formed while the last steps and the epilogue of this one run,
 // and its rows' key intervals arrive meanwhile.  8K tokens x 32 heads of 128 in
-// documents of 1024, mask alone: 109 -> 76 us, capped 134 -> 97; heads of 64 91 ->
-// 66 and 111 -> 90.  In a step that needs masking, 16-key chunks that no row of the
+// eight equal documents, mask alone: 109 -> 76 us (by now 72), capped at 50, which
+// no score came near, 134 -> 97; heads of 64 91 -> 66 and 111 -> 90 (64, 86).  In
+// documents of random lengths about 1024, a cap of 20 reached: 185-205 us by where
+// they lie.  In a step that needs masking, 16-key chunks that no row of the
 // warp sees are skipped.
 // Every wait is bounded (2 s), as in the plain forward.
 #include <cuda_bf16.h>
@@ -465,11 +467,13 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, 1)
       // its warp no masking, and written as O = 0, LSE = -inf.
       const int k_lo = keys.y == 0 ? -(1 << 29) : keys.x, k_hi = keys.y == 0 ? 1 << 29 : keys.x + keys.y;
       float m_used = kWide ? 0.f : -INFINITY, l = 0.f;  // the row's reference (base 2) and sum
-      // wide: what the rounded P of masked steps add to that.  A row's few first
-      // keys have no reference that makes the largest P 1, so O of a row that sees
-      // one key would be off by P's rounding: it is divided by the sum of what V
-      // was multiplied by.  (In other steps 64 keys and more share the error.  This
-      // costs 8K tokens x 32 heads in documents of 1024 170 -> 183 us.)
+      // wide: what the rounded P of masked steps add to that.  No reference makes a
+      // row's largest P 1, so its rounding, up to 2^-8 of it, would stay in O of a
+      // row that sees one key: O is divided by the sum of what V was multiplied by.
+      // In other steps it does stay: where one key of many carries a row, O is off
+      // by as much, as in the narrow form once a row's maximum has left its
+      // reference behind.  (This costs 8K tokens x 32 heads in documents of random
+      // lengths about 1024 170 -> 183 us.)
       float l_off = 0.f, lse_sum = 0.f;
       int form = 0;  // the form of tanh this warp's tiles have needed so far
       // The MMA issuer waits for P_x(t)'s arrivals alone; when that burst is the
@@ -529,8 +533,9 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, 1)
                             f2_of(__uint_as_float(s[2 * e + 2]), __uint_as_float(s[2 * e + 3]))};
                 if constexpr (kForm == 2) {
                   // (four scores share a reciprocal, and what is unseen may be NaN.  202 ->
-                  // 212 us in documents of 1024, 8K tokens x 32 heads, all in this form; a
-                  // look whether any is NaN first, or another pass if one was: 215-228.)
+                  // 212 us in documents of random lengths about 1024, 8K tokens x 32 heads,
+                  // all in this form; a look whether any is NaN first, or another pass if
+                  // one was: 215-228.)
                   if constexpr (kMask) any.drop_unseen(v[0], v[1], seen >> (2 * e));
                   any(v[0], v[1]);
                 }

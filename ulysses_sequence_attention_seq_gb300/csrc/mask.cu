@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(256) mask_order_kernel(const BuildParams p) {
 
 // Up to kMiddle tokens: a cluster of blocks a batch row, 1024 tokens a block, and
 // barriers of the cluster where the kernels above end; what they hand on goes
-// through the plan itself.  2060 tokens x 2 10 us, 8192 12 us; the four launches
+// through the plan itself.  2060 tokens x 2 9 us, 8192 11 us; the four launches
 // above take as long one behind the other, but 21 us called one by one.
 constexpr int kMiddle = 8 * kSmall;
 
