@@ -539,8 +539,8 @@ int ulysses_mask_build(const ulysses_problem *prob, const int32_t *doc, const in
  *   over the keys that row i sees by the mask plan (NULL: by prob->causal).
  * softcap: 0, or from 2^-10 to 2^20 (else ULYSSES_ERR_ARG).  slopes: device,
  * float [n_head], on a 16-byte boundary like every pointer (a slice of a larger
- * array that is not: ULYSSES_ERR_ALIGN).  mask: a plan of ulysses_mask_build with mask_bytes bytes
- * (too few: ULYSSES_ERR_WORKSPACE).
+ * array that is not: ULYSSES_ERR_ALIGN).  mask: a plan of ulysses_mask_build
+ * with mask_bytes bytes (too few: ULYSSES_ERR_WORKSPACE).
  */
 typedef struct ulysses_score_mod {
   float softcap;

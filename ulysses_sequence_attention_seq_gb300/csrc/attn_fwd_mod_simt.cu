@@ -343,7 +343,8 @@ cudaError_t launch_attn_fwd_mod_simt(const ulysses_problem &p, const float *q, c
                                      cudaStream_t st) {
   SimtParams sp{};
   sp.q = q, sp.k = k, sp.v = v, sp.o = o, sp.lse = lse;
-  sp.S = p.S, sp.B = p.B, sp.n_head = p.n_head, sp.hp = p.n_head / p.P, sp.kvp = kv_per_rank(p), sp.group = sp.hp / sp.kvp;
+  sp.S = p.S, sp.B = p.B, sp.n_head = p.n_head;
+  sp.hp = p.n_head / p.P, sp.kvp = kv_per_rank(p), sp.group = sp.hp / sp.kvp;
   sp.causal = p.causal;
   const float scale = p.softmax_scale > 0.f ? p.softmax_scale : 1.0f / sqrtf((float)p.head_dim);
   sp.scale_log2 = scale * 1.4426950408889634f;
